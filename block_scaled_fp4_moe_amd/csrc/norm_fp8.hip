@@ -248,24 +248,31 @@ __global__ __launch_bounds__(1024) void rms_norm_wide_kernel(NormParams p, int M
 
 // e^-g for SiLU: 2^t with t = -g*log2(e) carried as a rounded product and its
 // remainder, because the rounding of t alone would cost |t| * 2^-24 of relative
-// error; then 1/(1 + e^-g).  e^-g overflowing to infinity gives 0, and
-// g = -infinity gives -infinity * 0 = NaN, as the formula does.
-__device__ __forceinline__ float silu(float g) {
+// error; then 1/(1 + e^-g).
+//
+// Lanes with a gate beyond +-80 (or a NaN) are added to `far`: their block takes the 64-bit
+// form.  The remainder is left out there, and from -87.3 on the reciprocal is
+// subnormal, which the instruction returns as zero.  (The comparison is the select's own,
+// and the masks are joined by the scalar unit.)
+__device__ __forceinline__ float silu(float g, uint64_t& far) {
   const float L = 1.44269502f, L_lo = 1.92596299e-8f;   // log2(e) in two parts
   const float t = -g * L;
   const float lo = fmaf(-g, L, -t) - g * L_lo;
   float e = __builtin_amdgcn_exp2f(t);
   const float c = e * (lo * 0.693147181f);
-  e = fabsf(g) < 80.f ? e + c : e;                      // beyond, the remainder may be inf - inf
+  const bool beyond = !(fabsf(g) <= 80.f);
+  far |= __ballot(beyond);
+  e = beyond ? e : e + c;                               // there the remainder may be inf - inf
   const float d = 1.f + e;
   float r = __builtin_amdgcn_rcpf(d);
   return g * r;
 }
 
-// The same in 64 bits, to about 2^-32: 2^n * 2^f with n the integer next to
+// The same in 64 bits and for any gate, to about 2^-32: 2^n * 2^f with n the integer next to
 // -g*log2(e), and 2^f = e^(f ln 2) by its series up to the eighth power (|f| <= 1/2 leaves
-// (ln 2/2)^9/9!).  The exponent's gate is cut at +-700: beyond, 1 + e^-g is 1 or larger than any
-// product of two floats.
+// (ln 2/2)^9/9!).  The exponent's gate is cut at 700: beyond, 1 + e^-g is 1.  Gates below
+// -108.67, whose SiLU is less than half of the smallest float32, give -0, and -infinity
+// gives -infinity * 0 = NaN, as the formula does.
 __device__ __forceinline__ double silu64(float g) {
   const double t = -1.4426950408889634 * (double)__builtin_amdgcn_fmed3f(g, -700.f, 700.f);
   const double n = __builtin_rint(t), f = t - n;
@@ -279,9 +286,12 @@ __device__ __forceinline__ double silu64(float g) {
   e = fma(e, f, 6.9314718055994531e-01);
   e = fma(e, f, 1.0);
   const double d = 1.0 + __builtin_amdgcn_ldexp(e, (int)n);
-  const double r = __builtin_amdgcn_rcp(d);
-  return (double)g * fma(fma(-d, r, 1.0), r, r);
+  const double r = __builtin_amdgcn_rcp(d), q = fma(fma(-d, r, 1.0), r, r);
+  return (double)g * (g < -108.67f ? 0.0 : q);
 }
+
+// Whether a block's largest magnitude (its bits) lies in 2^-55 .. 2^100.
+__device__ __forceinline__ bool usual(uint32_t m) { return m >= 0x24000000u && m <= 0x71800000u; }
 
 // Scale and codes of a block of h = silu(g)*u from 64-bit values.
 __device__ __forceinline__ float quant8_swiglu64(const float* g, const float* u, uint32_t* c) {
@@ -294,7 +304,9 @@ __device__ __forceinline__ float quant8_swiglu64(const float* g, const float* u,
     p[i] = (float)h[i];
     top = max(top, __float_as_uint(p[i]) & 0x7fffffffu);
   }
-  const float m = __uint_as_float(row16_max(top));
+  top = row16_max(top);
+  if (!usual(top)) return quant8_e4m3(p, c);
+  const float m = __uint_as_float(top);
   float lo = -__builtin_inff();     // what the largest value's float32 form leaves out
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -330,14 +342,17 @@ __device__ __forceinline__ float quant8_swiglu64(const float* g, const float* u,
 __device__ __forceinline__ float quant8_swiglu(const float* g, const float* u, uint32_t* c) {
   float h[8];
   uint32_t m = 0;
+  uint64_t far = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    h[i] = silu(g[i]) * u[i];
+    h[i] = silu(g[i], far) * u[i];
     m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
   }
   m = row16_max(m);
-  const bool usual = m >= 0x24000000u && m <= 0x71800000u;      // 2^-55 .. 2^100
-  if (!usual) return quant8_e4m3(h, c);
+  // the block's own lanes decide, so that a row's result does not depend on its neighbours
+  auto own = [](uint64_t lanes) { return ((lanes >> (threadIdx.x & 48)) & 0xffff) != 0; };
+  if (far && own(far)) return quant8_swiglu64(g, u, c);
+  if (!usual(m)) return quant8_e4m3(h, c);
   const float f = 448.f * __builtin_amdgcn_rcpf(__uint_as_float(m));
   constexpr uint32_t kUnits = 12;
   uint32_t near = ~0u;              // units above the middle of two codes less kUnits
@@ -346,9 +361,8 @@ __device__ __forceinline__ float quant8_swiglu(const float* g, const float* u, u
     h[i] *= f;
     near = min(near, (__float_as_uint(h[i]) - (0x80000u - kUnits)) & 0xfffffu);
   }
-  // the block's own lanes decide, so that a row's result does not depend on its neighbours
   const uint64_t hit = __ballot(near <= 2 * kUnits);
-  if (hit && ((hit >> (threadIdx.x & 48)) & 0xffff)) return quant8_swiglu64(g, u, c);
+  if (hit && own(hit)) return quant8_swiglu64(g, u, c);
   e4m3_codes(h, c);
   return __fdiv_rn(__uint_as_float(m), 448.f);
 }

@@ -83,8 +83,8 @@ int rms_norm_fp8(const fp8block_norm_args* args, void* stream);
 /*
  * swiglu_fp8 -- h = SiLU(gate) * up, quantized 1x128.
  * gate_up [M, 2I] of `dtype`, row stride ldg: gate in columns [0, I), up in
- * [I, 2I).  h is not rounded in between; SiLU of a gate below -88 is -0, as in
- * float32.  codes [M, I] bytes, row stride ldc; scales [M, ceil(I/128)].
+ * [I, 2I).  h is not rounded in between; SiLU of a gate below -108.67, less than half
+ * of the smallest float32, is -0.  codes [M, I] bytes, row stride ldc; scales [M, ceil(I/128)].
  * row_count (device, NULL = M): rows at or past it are not written.  M >= 0, I >= 1, M * ceil(I/128) < 2^31.
  */
 int swiglu_fp8(int dtype, const void* gate_up, int M, int I, int64_t ldg,
