@@ -47,12 +47,16 @@ __device__ __forceinline__ float wave_sum(float v) {
   return (row(0) + row(16)) + (row(32) + row(48));
 }
 
-// 1/sqrt(m) to about one unit: the instruction's value and one Newton step on it.
+// 1/sqrt(m) to about one unit: the instruction's value and one Newton step on it.  The
+// instruction takes a subnormal m for zero: small ones are brought up by 2^64 before.
 __device__ __forceinline__ float rsqrt_refined(float m) {
-  const float r = __builtin_amdgcn_rsqf(m);
+  const bool small = m < 0x1p-100f;
+  m = small ? m * 0x1p64f : m;
+  float r = __builtin_amdgcn_rsqf(m);
   const float e = fmaf(-m * r, r, 1.f);
   // m = 0 or infinity: r is infinity or 0 and e a NaN; a NaN m stays one
-  return (r > 0.f && r < __builtin_inff()) ? fmaf(0.5f * r, e, r) : r;
+  r = (r > 0.f && r < __builtin_inff()) ? fmaf(0.5f * r, e, r) : r;
+  return small ? r * 0x1p32f : r;
 }
 
 // Scale and codes of a block of y = v*inv*w.  The row's factor inv cancels in

@@ -5,8 +5,8 @@ import numpy as np
 import pytest
 import torch
 
-from .test_gpu_fp8_block import (DTYPES, NORM, SILU, check_product, check_quantized, gen,
-                                 quantized_pair, randn, silu_mul64)
+from .test_gpu_fp8_block import (DTYPES, NORM, SILU, check_product, check_quantized,
+                                 check_rounded, gen, quantized_pair, randn, silu_mul64)
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,28 @@ def test_swiglu_low_gates_do_not_depend_on_the_path(gpu_lib):
     c, s = gpu_lib.swiglu_fp8(gu)
     assert np.all(np.abs(s.double().cpu().numpy() * 448 / want - 1) <= SILU + 2.0 ** -23)
     check_quantized(c, s, silu_mul64(gu), SILU, "path")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [256, 20480])
+def test_norm_of_rows_with_a_subnormal_mean_square(gpu_lib, K, dtype):
+    """Powers of two without eps: squares and their sums are exact, y = sign(x) * weight."""
+    g = gen(52)
+    size = 2.0 ** torch.tensor([[-60.0], [-66.0], [-69.0], [-72.0]])
+    x = (torch.sign(randn(g, 4, K)) * size).to(DTYPES[dtype]).cuda()
+    w = (1 + 0.3 * randn(g, K)).to(DTYPES[dtype]).cuda()
+    y = torch.empty_like(x)
+    c, s, _ = gpu_lib.rms_norm_fp8(x, w, eps=0.0, y=y)
+    ref = torch.sign(x).double().cpu().numpy() * w.double().cpu().numpy()
+    check_quantized(c, s, ref, NORM, "subnormal")
+    check_rounded(y, ref, NORM * np.abs(ref), "y")
+
+
+def test_norm_of_a_zero_row_without_eps(gpu_lib):
+    """0 / 0: NaN throughout, as the formula gives; the row beside it is not touched by it."""
+    x = torch.ones((2, 256), device="cuda")
+    x[0] = 0
+    c, s, _ = gpu_lib.rms_norm_fp8(x, torch.ones(256, device="cuda"), eps=0.0)
+    q = c.view(torch.float8_e4m3fn).float()
+    assert bool(s[0].isnan().all()) and bool(q[0].isnan().all())
+    assert bool((q[1] == 448).all())
