@@ -114,7 +114,7 @@ __global__ __launch_bounds__(NW * 64) void skinny_kernel(Block8Params p, int64_t
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
   // work items: row tile outer, weight rows inner
-  const int n_blocks = (p.N + 15) / 16;
+  const int n_blocks = (p.N - 1) / 16 + 1;      // N may be the largest int
   for (int64_t item = blockIdx.x; item < tiles * n_blocks; item += gridDim.x) {
     RowTile rt;
     if (!find_tile(p, (int)(item / n_blocks), 16, rt)) continue;

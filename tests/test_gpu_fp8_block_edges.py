@@ -62,3 +62,23 @@ def test_norm_of_a_zero_row_without_eps(gpu_lib):
     q = c.view(torch.float8_e4m3fn).float()
     assert bool(s[0].isnan().all()) and bool(q[0].isnan().all())
     assert bool((q[1] == 448).all())
+
+
+@pytest.mark.parametrize("N", [2 ** 24 + 40, 2 ** 31 - 8, 2 ** 31 - 1])
+def test_linear_up_to_the_largest_row_count(gpu_lib, N):
+    """More items than a grid holds, and N next to 2^31: sampled weight rows from the whole
+    range, the first turn of the item loop and the last."""
+    if torch.cuda.mem_get_info()[0] < N * 20:
+        pytest.skip("not enough free memory")
+    a, sa, w16, sw = quantized_pair(gen(7), 1, 64, 16, whole=True)
+    w = torch.zeros((N, 16), dtype=torch.uint8, device="cuda")
+    at = torch.tensor([0, 17, 2 ** 23 + 5, 2 ** 24 + 16, N - 30, N - 9, N - 8, N - 2, N - 1], device="cuda")
+    w[at] = w16[:9]
+    one = sw[:1].expand((N + 127) // 128, 1)
+    out = torch.full((1, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    gpu_lib.fp8_block_linear(a, sa, w, one, out=out)
+    check_product(out[:, at], a, sa, w16[:9], sw, "rows", True)
+    for lo in range(0, N, 2 ** 28):
+        assert not bool((out[0, lo:lo + 2 ** 28] == 7.0).any())
+    del w, out
+    torch.cuda.empty_cache()
