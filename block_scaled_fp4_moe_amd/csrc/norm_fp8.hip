@@ -17,6 +17,8 @@
 // 128-value block, so the block maximum takes four DPP steps and no LDS.
 #include "fp8_block.h"
 
+#include <numeric>
+
 namespace fp4moe {
 namespace {
 
@@ -471,6 +473,17 @@ bool aligned(const void* p, int dtype) {
   return ((uintptr_t)p & (dtype == FP8BLOCK_F32 ? 3 : 1)) == 0;
 }
 
+// Whether the scales of M rows of K columns lie at places of their own.  Two elements
+// meet where i * row = j * blk with 0 < i < M and 0 < j < blocks, first at
+// i = blk / gcd, j = row / gcd (a stride of zero: at the next row or block).
+bool scales_apart(int64_t M, int64_t K, int64_t row, int64_t blk) {
+  const int64_t blocks = (K + 127) / 128;
+  if (M <= 1 || blocks <= 1) return (M <= 1 || row > 0) && (blocks <= 1 || blk > 0);
+  if (row == 0 || blk == 0) return false;
+  const int64_t g = std::gcd(row, blk);
+  return blk / g >= M || row / g >= blocks;
+}
+
 }  // namespace
 }  // namespace fp4moe
 
@@ -493,6 +506,9 @@ extern "C" int rms_norm_fp8(const fp8block_norm_args* a, void* stream) {
                  "rms_norm_fp8: a row stride is below K=%d", a->K);
   FP4MOE_REQUIRE(!a->scales || (a->scale_row >= 0 && a->scale_blk >= 0),
                  "rms_norm_fp8: negative scale stride");
+  FP4MOE_REQUIRE(!a->scales || scales_apart(a->M, a->K, a->scale_row, a->scale_blk),
+                 "rms_norm_fp8: scale strides %lld, %lld put scales on top of each other",
+                 (long long)a->scale_row, (long long)a->scale_blk);
   FP4MOE_REQUIRE(aligned(a->x, a->dtype) && aligned(a->residual, a->dtype) &&
                      aligned(a->weight, a->dtype) && aligned(a->residual_out, a->dtype) &&
                      aligned(a->y_out, a->dtype) && ((uintptr_t)a->scales & 3) == 0,
@@ -523,6 +539,9 @@ extern "C" int swiglu_fp8(int dtype, const void* gate_up, int M, int I, int64_t 
   FP4MOE_REQUIRE(ldg >= 2 * (int64_t)I && ldc >= I, "swiglu_fp8: ldg=%lld ldc=%lld for I=%d",
                  (long long)ldg, (long long)ldc, I);
   FP4MOE_REQUIRE(scale_row >= 0 && scale_blk >= 0, "swiglu_fp8: negative scale stride");
+  FP4MOE_REQUIRE(scales_apart(M, I, scale_row, scale_blk),
+                 "swiglu_fp8: scale strides %lld, %lld put scales on top of each other",
+                 (long long)scale_row, (long long)scale_blk);
   FP4MOE_REQUIRE(aligned(gate_up, dtype) && ((uintptr_t)scales & 3) == 0 &&
                      ((uintptr_t)row_count & 3) == 0,
                  "swiglu_fp8: a pointer is not aligned to its element");

@@ -15,7 +15,8 @@
  *     of its block.  Blocks are 128 wide along the row (K, or the output
  *     width); the last block of a row may be shorter.  KB = ceil(K/128).
  *   - Activation scales: element (row, block) at row*row_stride +
- *     block*blk_stride, any non-negative strides.  The kernels read the scales of
+ *     block*blk_stride, any non-negative strides (of an output: that put no two
+ *     elements in one place).  The kernels read the scales of
  *     consecutive rows of one block together, so row_stride 1 is the layout
  *     to prefer (what the Python binding allocates).
  *   - Weight scales: [ceil(N/128), KB], row stride given.

@@ -82,3 +82,11 @@ def test_linear_up_to_the_largest_row_count(gpu_lib, N):
         assert not bool((out[0, lo:lo + 2 ** 28] == 7.0).any())
     del w, out
     torch.cuda.empty_cache()
+
+
+def test_scales_on_top_of_each_other_are_refused(gpu_lib):
+    x, w = torch.ones((4, 256), device="cuda"), torch.ones(128, device="cuda")
+    with pytest.raises(gpu_lib.FP4MoEError):
+        gpu_lib.rms_norm_fp8(x[:, :128], w, scales=torch.empty((1, 1), device="cuda").expand(4, 1))
+    with pytest.raises(gpu_lib.FP4MoEError):
+        gpu_lib.swiglu_fp8(x, scales=torch.empty((1, 1), device="cuda").expand(4, 1))
