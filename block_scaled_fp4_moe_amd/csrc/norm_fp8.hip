@@ -484,6 +484,63 @@ bool scales_apart(int64_t M, int64_t K, int64_t row, int64_t blk) {
   return blk / g >= M || row / g >= blocks;
 }
 
+// `rows` pieces of `width` bytes, `pitch` apart.
+struct Piece {
+  uintptr_t at;
+  int64_t rows, pitch, width;
+  uintptr_t end() const { return at + (rows - 1) * pitch + width; }
+};
+
+// Whether two of them have a byte in common (null ones: no).  Exact where their pitches are
+// equal or one is a single row (columns of one buffer do not meet); otherwise whether the
+// ranges do.
+bool meet(const Piece& a, const Piece& b) {
+  if (!a.at || !b.at || a.end() <= b.at || b.end() <= a.at) return false;
+  if (a.rows > 1 && b.rows > 1 && a.pitch != b.pitch) return true;
+  const Piece &low = a.at <= b.at ? a : b, &high = a.at <= b.at ? b : a;
+  if (low.rows <= 1) return true;                      // the other one starts inside it
+  const int64_t d = (int64_t)((high.at - low.at) % (uintptr_t)low.pitch);
+  return d < low.width || d + high.width > low.pitch;
+}
+
+// Scales as rows, or, where the rows of a block lie together, as blocks.
+Piece scale_piece(const float* at, int64_t M, int64_t K, int64_t row, int64_t blk) {
+  const int64_t blocks = (K + 127) / 128;
+  const int64_t across = (blocks - 1) * blk + 1, down = (M - 1) * row + 1;
+  const uintptr_t p = (uintptr_t)at;
+  if (across <= row) return {p, M, row * 4, across * 4};
+  if (down <= blk) return {p, blocks, blk * 4, down * 4};
+  return {p, 1, 0, ((M - 1) * row + across) * 4};
+}
+
+// residual_out and y_out each lie on x or residual, row for row, or apart from every
+// input; codes and scales apart from everything.  Rows are read and written by
+// workgroups in any order, so anything else would be a race.
+const char* overlap(const fp8block_norm_args* a) {
+  const int64_t E = a->dtype == FP8BLOCK_F32 ? 4 : 2;
+  auto rows = [&](const void* p, int64_t ld, int64_t e) {
+    return Piece{(uintptr_t)p, a->M, ld * e, a->K * e};
+  };
+  const Piece in[] = {rows(a->x, a->ldx, E), rows(a->residual, a->ldr, E)};
+  const Piece weight = {(uintptr_t)a->weight, 1, 0, a->K * E};
+  const Piece out[] = {rows(a->residual_out, a->ldro, E), rows(a->y_out, a->ldy, E)};
+  const Piece code[] = {rows(a->codes, a->ldc, 1),
+                        scale_piece(a->scales, a->M, a->K, a->scale_row, a->scale_blk)};
+  const char* names[] = {"residual_out", "y_out", "codes", "scales"};
+  for (int o = 0; o < 2; ++o) {
+    for (const Piece& i : in) {
+      const bool same = out[o].at == i.at && (a->M == 1 || out[o].pitch == i.pitch);
+      if (!same && meet(out[o], i)) return names[o];
+    }
+    if (meet(out[o], weight)) return names[o];
+    for (const Piece& i : in)
+      if (meet(code[o], i)) return names[2 + o];
+    if (meet(code[o], weight) || meet(code[o], out[0]) || meet(code[o], out[1])) return names[2 + o];
+  }
+  if (meet(code[0], code[1])) return names[3];
+  return meet(out[0], out[1]) ? names[1] : nullptr;
+}
+
 }  // namespace
 }  // namespace fp4moe
 
@@ -513,6 +570,8 @@ extern "C" int rms_norm_fp8(const fp8block_norm_args* a, void* stream) {
                      aligned(a->weight, a->dtype) && aligned(a->residual_out, a->dtype) &&
                      aligned(a->y_out, a->dtype) && ((uintptr_t)a->scales & 3) == 0,
                  "rms_norm_fp8: a pointer is not aligned to its element");
+  const char* on = overlap(a);
+  FP4MOE_REQUIRE(!on, "rms_norm_fp8: %s overlaps an input or another output", on);
   FP4MOE_CHECK_DEVICE();
   NormParams p;
   p.x = a->x, p.residual = a->residual, p.weight = a->weight;

@@ -54,8 +54,9 @@ def rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, 
     x, residual [M, K] and weight [K] of one dtype (bfloat16, float16 or
     float32).  Returns (codes uint8 [M, K], scales float32 [M, ceil(K/128)],
     residual_out): residual_out is v rounded to the dtype (None without a
-    residual; a new tensor unless one is passed, which may be x or residual).
-    y: a tensor that receives the normalised rows in the dtype."""
+    residual; a new tensor unless one is passed).  y: a tensor that receives the
+    normalised rows in the dtype.  residual_out and y may each be x or residual itself;
+    any other overlap of an output is refused."""
     return _on(stream, x, _native.rms_norm_fp8, x, weight, eps, residual, residual_out, y, codes,
                scales)
 

@@ -54,8 +54,8 @@ enum {
  *   the other outputs are written).
  * x, residual, residual_out, y_out: [M, K] of `dtype`, row strides in
  * elements (>= K).  weight [K] of `dtype`.  codes [M, K] bytes with row stride
- * ldc, scales [M, KB].  residual_out may be x or residual itself (same stride);
- * other overlaps of outputs and inputs are not allowed.  M >= 0,
+ * ldc, scales [M, KB].  residual_out and y_out may each be x or residual itself (same
+ * stride); other overlaps of an output with an input or another output are refused.  M >= 0,
  * 1 <= K <= 65536.
  * Any alignment of whole elements is accepted; rows whose pointers and strides
  * are all 16-byte multiples (codes: 8) are the fastest.

@@ -40,3 +40,47 @@ def test_scales_of_an_output_lie_apart(M, K, row, blk, apart):
     assert (st == 1) == (not apart)
     if not apart:
         assert "swiglu_fp8: scale strides" in _message()
+
+
+X, R, W, C, S, O = (i << 24 for i in range(1, 7))        # far apart
+
+
+def packed(**kw):
+    """Rows of 64 bfloat16 (128 bytes), four of them, everything apart."""
+    a = dict(M=4, K=64, x=X, ldx=64, residual=R, ldr=64, weight=W, codes=C, ldc=64, scales=S,
+             scale_row=1, scale_blk=4)
+    a.update(kw)
+    return norm(**a)
+
+
+@pytest.mark.parametrize("fine", [
+    dict(), dict(residual_out=X, ldro=64), dict(residual_out=R, ldro=64), dict(y_out=X, ldy=64),
+    dict(residual_out=R, ldro=64, y_out=X, ldy=64), dict(residual_out=O, ldro=80),
+    # column ranges of one buffer, in any order
+    dict(ldx=200, residual_out=X + 128, ldro=200), dict(x=X + 272, ldx=200, residual_out=X, ldro=200),
+    dict(ldx=200, codes=X + 128, ldc=400, scales=X + 192, scale_row=100),
+    # behind the last row, before the first
+    dict(residual_out=X + 512, ldro=64), dict(residual_out=X - 512, ldro=64),
+    dict(ldx=100, residual_out=X + 728, ldro=64), dict(weight=X + 512), dict(weight=X - 128),
+    # of a single row the stride says nothing
+    dict(M=1, residual_out=X, ldro=99), dict(ldx=200, weight=X + 128),
+    dict(codes=C, scales=C + 256), dict(codes=C, ldc=68, scales=C + 64, scale_row=17),
+    dict(codes=None, scales=None, y_out=O, ldy=64)])
+def test_norm_takes_outputs_that_lie_apart_or_on_an_input(fine):
+    assert packed(**fine) != 1, _message()
+
+
+@pytest.mark.parametrize("bad,which", [
+    (dict(residual_out=X, ldro=72), "residual_out"), (dict(residual_out=R, ldro=128), "residual_out"),
+    (dict(residual_out=X + 128, ldro=64), "residual_out"), (dict(residual_out=X - 384, ldro=64), "residual_out"),
+    (dict(residual_out=X + 2, ldro=64), "residual_out"), (dict(ldx=200, residual_out=X + 126, ldro=200), "residual_out"),
+    (dict(ldx=200, residual_out=X + 274, ldro=200), "residual_out"),
+    (dict(y_out=X + 2, ldy=64), "y_out"), (dict(y_out=W - 510, ldy=64), "y_out"),
+    (dict(residual_out=O, ldro=64, y_out=O, ldy=64), "y_out"),
+    (dict(codes=X), "codes"), (dict(codes=W + 127), "codes"), (dict(codes=R + 511), "codes"),
+    (dict(residual_out=O, ldro=64, codes=O + 511), "codes"),
+    (dict(scales=X + 508), "scales"), (dict(scales=C), "scales"), (dict(scales=C + 252), "scales"),
+    (dict(codes=C, ldc=68, scales=C + 60, scale_row=17), "scales"),
+    (dict(y_out=O, ldy=64, scales=O - 12), "scales")])
+def test_norm_refuses_other_overlaps(bad, which):
+    assert packed(**bad) == 1 and f"rms_norm_fp8: {which} overlaps" in _message()

@@ -90,3 +90,20 @@ def test_scales_on_top_of_each_other_are_refused(gpu_lib):
         gpu_lib.rms_norm_fp8(x[:, :128], w, scales=torch.empty((1, 1), device="cuda").expand(4, 1))
     with pytest.raises(gpu_lib.FP4MoEError):
         gpu_lib.swiglu_fp8(x, scales=torch.empty((1, 1), device="cuda").expand(4, 1))
+
+
+@pytest.mark.parametrize("K,M", [(640, 12), (7168, 300), (20480, 3)])
+def test_norm_y_and_residual_in_place(gpu_lib, K, M):
+    """y on x and residual_out on residual at once, in every kind of kernel; an output
+    that is shifted against its input is refused."""
+    g = gen(K)
+    x, r = randn(g, M, K).bfloat16().cuda(), randn(g, M, K).bfloat16().cuda()
+    w = (1 + 0.3 * randn(g, K)).bfloat16().cuda()
+    y = torch.empty_like(x)
+    c, s, ro = gpu_lib.rms_norm_fp8(x, w, residual=r, y=y)
+    x2, r2 = x.clone(), r.clone()
+    c2, s2, ro2 = gpu_lib.rms_norm_fp8(x2, w, residual=r2, residual_out=r2, y=x2)
+    assert ro2 is r2 and torch.equal(r2, ro) and torch.equal(x2, y)
+    assert torch.equal(c, c2) and torch.equal(s, s2)
+    with pytest.raises(gpu_lib.FP4MoEError):
+        gpu_lib.rms_norm_fp8(x[:-1], w, residual=r[:-1], residual_out=r[1:])
