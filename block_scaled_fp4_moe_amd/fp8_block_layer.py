@@ -20,6 +20,13 @@ from . import (fp8_block_grouped_gemm, fp8_block_linear, moe_combine, moe_permut
                rms_norm_fp8, swiglu_fp8)
 
 
+def _check_x(x, dtypes, wanted):
+    """Before anything is launched: the products return 16-bit types only, the combine
+    bfloat16."""
+    if x.dtype not in dtypes:
+        raise ValueError(f"x is {x.dtype}; wanted {wanted}")
+
+
 class FP8BlockMLP:
     """norm [H]; w13 codes [2I, H] (gate rows first), w13_scale [2I/128, H/128]; w2
     codes [H, I], w2_scale [H/128, I/128] (block counts rounded up)."""
@@ -29,7 +36,9 @@ class FP8BlockMLP:
         self.w13, self.w13_scale, self.w2, self.w2_scale = w13, w13_scale, w2, w2_scale
 
     def forward(self, x, residual=None, stream=None):
-        """x, residual [T, H] -> (out [T, H] of x's type, the new residual or None)."""
+        """x, residual [T, H] bfloat16 or float16, of norm's type -> (out [T, H] of x's
+        type, the new residual or None)."""
+        _check_x(x, (torch.bfloat16, torch.float16), "bfloat16 or float16")
         codes, scales, residual = rms_norm_fp8(x, self.norm, self.eps, residual, stream=stream)
         gate_up = fp8_block_linear(codes, scales, self.w13, self.w13_scale, out_dtype=x.dtype,
                                    stream=stream)
@@ -65,6 +74,7 @@ class FP8BlockMoE:
         """x, residual bfloat16 [T, H], logits float32 [T, E] (None: the router's own)
         -> (out bfloat16 [T, H], the new residual or None), on the current stream.
         keep=True: a dict of every intermediate instead."""
+        _check_x(x, (torch.bfloat16,), "bfloat16")
         c = self.cfg
         k = c.topk + c.n_shared
         y = torch.empty_like(x) if logits is None else None
