@@ -53,12 +53,9 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
          t.strides(), "; wanted ", wanted);
 }
 
-// Row stride of a matrix; of a single row at least the row's length (torch keeps any
-// number there).
-int64_t ld(const at::Tensor& t) {
-  const int64_t s = t.stride(-2), rows = t.size(-2), cols = t.size(-1);
-  return rows > 1 || s > cols ? s : cols;
-}
+// Row stride of a matrix; of a single row, whose stride means nothing (torch keeps any
+// number there), the row's length.
+int64_t ld(const at::Tensor& t) { return t.size(-2) > 1 ? t.stride(-2) : t.size(-1); }
 
 bool rows_contiguous(const at::Tensor& t) { return t.size(-1) <= 1 || t.stride(-1) == 1; }
 

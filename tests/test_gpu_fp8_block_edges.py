@@ -107,3 +107,25 @@ def test_norm_y_and_residual_in_place(gpu_lib, K, M):
     assert torch.equal(c, c2) and torch.equal(s, s2)
     with pytest.raises(gpu_lib.FP4MoEError):
         gpu_lib.rms_norm_fp8(x[:-1], w, residual=r[:-1], residual_out=r[1:])
+
+
+def test_a_single_row_may_have_any_stride(gpu_lib):
+    """One row cut out of a buffer whose rows are not 16 bytes apart, on every side."""
+    a, sa, w, sw = quantized_pair(gen(1), 2, 40, 256)
+
+    def cut(t, pad):
+        room = torch.zeros((t.shape[0], t.shape[1] + pad), dtype=t.dtype, device="cuda")
+        room[:, :t.shape[1]] = t
+        return room[:1, :t.shape[1]]
+
+    want = gpu_lib.fp8_block_linear(a, sa, w, sw)
+    out = torch.zeros((1, 43), dtype=torch.bfloat16, device="cuda")[:, :40]
+    got = gpu_lib.fp8_block_linear(cut(a, 4), cut(sa, 1), w, cut(sw, 3), out=out)
+    assert got is out and torch.equal(got, want[:1])
+    assert torch.equal(gpu_lib.fp8_block_linear(a, sa, cut(w, 12), sw), want[:, :1])
+    perm = dict(expert_offsets=torch.tensor([0, 1], dtype=torch.int32, device="cuda"),
+                sorted_pairs=torch.zeros(1, dtype=torch.int32, device="cuda"),
+                tiles=torch.zeros((1, 2), dtype=torch.int32, device="cuda"),
+                n_tiles=torch.ones(1, dtype=torch.int32, device="cuda"), max_tiles=1)
+    got = gpu_lib.fp8_block_grouped_gemm(cut(a, 4), cut(sa, 1), cut(w, 12)[None], sw[None], perm, 16)
+    assert torch.equal(got, want[:1, :1])
