@@ -129,3 +129,14 @@ def test_a_single_row_may_have_any_stride(gpu_lib):
                 n_tiles=torch.ones(1, dtype=torch.int32, device="cuda"), max_tiles=1)
     got = gpu_lib.fp8_block_grouped_gemm(cut(a, 4), cut(sa, 1), cut(w, 12)[None], sw[None], perm, 16)
     assert torch.equal(got, want[:1, :1])
+
+
+def test_an_output_that_does_not_fit(gpu_lib):
+    """torch's own out-of-memory error, as from any allocation; the next call works."""
+    a = torch.zeros((1, 256), dtype=torch.uint8, device="cuda").expand(2 ** 31 - 1, 256)
+    sa = torch.ones((1, 2), device="cuda").expand(2 ** 31 - 1, 2)
+    w = torch.zeros((8192, 256), dtype=torch.uint8, device="cuda")
+    sw = torch.ones((64, 2), device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        gpu_lib.fp8_block_linear(a, sa, w, sw)               # 32 TiB
+    assert not bool(gpu_lib.fp8_block_linear(a[:3].contiguous(), sa[:3], w, sw).any())
