@@ -96,8 +96,8 @@ __device__ __forceinline__ int a_row_of(const Block8Params& p, int r) {
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: weights stream from memory once and set the time (1 x 4096 x 7168: 8.0 us,
-// 3.7 TB/s; of it a launch, one memory latency and the join).
+// Few rows: weights stream from memory once and set the time (1 x 4096 x 7168: 7.6 us,
+// 3.9 TB/s; of it a launch, one memory latency and the join).
 //
 // A workgroup owns 16 weight rows x 16 activation rows; its NW waves take the
 // 128-wide K blocks in turn, U of them in flight each, and their sums are joined
@@ -200,8 +200,8 @@ __global__ __launch_bounds__(NW * 64) void skinny_kernel(Block8Params p, int64_t
 //
 // Measured: 16384 x 7168 x 7168 0.71 to 0.73 ms = 2.3 to 2.4 PFLOP/s, the matrix units busy 64% of the
 // cycles at 1.8 GHz (power sets the clock); 8192 tokens over 384 + 1 experts of 4096 x 7168
-// 3.4 ms, bound by weights (19.5 GB leave L2, 5.7 TB/s); 8 tokens over the same 0.31 ms =
-// 5.8 TB/s; 64 x 7168 x 2048 7.2 us, latencies.
+// 3.45 ms, bound by weights (19.5 GB leave L2, 5.7 TB/s); 8 tokens over the same 0.31 ms =
+// 5.8 TB/s; 64 x 7168 x 2048 7.0 us, latencies.
 //
 // A K block of a row is 128 bytes, one cache line: rows are copied to LDS as they
 // are (global_load_lds_dwordx4, eight rows an instruction), two buffers deep.
@@ -622,22 +622,23 @@ __global__ __launch_bounds__(KG * WM * WN * 64, OCC) void tile_kernel(Block8Para
   }
 }
 
-// Workgroups of one launch at most (a HIP grid holds fewer than 2^32 threads);
-// the kernels step over the rest of their items.
+// Workgroups of one launch at most (a HIP grid holds fewer than 2^32 threads).  A
+// workgroup of the tile kernel takes one item, so products of more items go to the 16x16
+// kernel, which steps over the rest of its own.
 constexpr int64_t kMaxGrid = 1 << 20;
 
 // Which kernel takes a product.  Measured on MI355X (us a launch; bfloat16 out, weights
 // from memory; "x3" K groups, "w3" three weight buffers):
 //
 // dense 4096 x 7168   M=16    64   128   256   512  1024  2048  4096
-//   16x16                11    30    55
-//   64x32 x6             14    17    17    30    46
-//   64x64 x4                   24    24    24    36    78
-//   64x128 x3                  37    36    35    26    51   102
-//   128x128 x2                             43    32    36    71
-//   128x256 w3                                         47    59   118
-//   192x256 w3                                         62    69   147
-//   256x256                                            80    84   107
+//   16x16                11    29    66
+//   64x32 x6             14    17    17    30    55
+//   64x64 x4                   24    23    23    43    81
+//   64x128 x3                  35    34    33    34    63   124
+//   128x128 x2                             43    44    45    84
+//   128x256 w3                                         53    61   122
+//   192x256 w3                                         67    75   141
+//   256x256                                            90    92   107
 // A tile shape is best up to one workgroup on each of the 256 CUs, then the next one;
 // the same held at 7168 x 2048, 1000 x 2000 and 576 x 7168.  With few K blocks there is
 // nothing for K groups to take in parallel: 64x128 alone (2048 x 512: M=256 4.9 against
@@ -651,6 +652,7 @@ constexpr int64_t kMaxGrid = 1 << 20;
 //   128x256 w3          997  1664  2190  2199  2679  3747
 //   192x256 w3         1013  1689  2240  2161  2643  3643
 //   256x256            1182  1971  2634  2480  2902  3869
+// (Averages above these were not timed and take the last row's shape.)
 // Few tiles: 16x16 (9 tiles x 32 column blocks of 128: 56 against 63 for 64x128), K groups
 // (15 x 32: 49 against 63).
 template <class Out>

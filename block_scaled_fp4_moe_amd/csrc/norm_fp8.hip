@@ -4,14 +4,13 @@
 // 128 values s = max(amax/448, 2^-64), code = E4M3(y/s).  One pass: a workgroup
 // owns a row and keeps v in registers between the sum of squares and the
 // quantization, so each input byte is read once (rows above 16384 columns twice).
-// Bound by HBM at prefill sizes, 8192 x 7168 bfloat16 with a residual 85 us = 4.9 TB/s,
-// a copy's rate; by launch and three latencies (load, cross-wave sum, store) at decode
-// sizes, 8 x 7168 5.1 us.
+// Bound by HBM at prefill sizes, 8192 x 7168 bfloat16 with a residual 86 us = 4.8 TB/s
+// (a bare stream of the same four bytes read to three written: 5.8); by launch and three
+// latencies (load, cross-wave sum, store) at decode sizes, 8 x 7168 5.0 us.
 //
 // swiglu_fp8: h = g / (1 + e^-g) * u, quantized the same way, in float32 and in 64 bits where
-// a code hangs on it.  Bound by HBM, 73728 x 2048
-// bfloat16 137 us = 5.3 TB/s with four bytes read for one written; by the launch at decode
-// sizes, 72 x 2048 3.1 us.
+// a code hangs on it.  Bound by HBM, 73728 x 2048 bfloat16 137 us = 5.5 TB/s with four bytes
+// read for one written (a bare stream: 6.3); by the launch at decode sizes, 72 x 2048 3.8 us.
 //
 // In both, a lane holds 8 consecutive values and the 16 lanes of a DPP row one
 // 128-value block, so the block maximum takes four DPP steps and no LDS.

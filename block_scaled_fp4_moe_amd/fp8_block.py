@@ -8,8 +8,9 @@
 Signatures only: the native module _fp8_block checks the arguments (ValueError),
 allocates outputs that are not passed in and calls the library (FP4MoEError for
 what that refuses).  Codes are uint8 or torch.float8_e4m3fn tensors; activation
-scales are float32 [rows, ceil(K/128)] tensors of any strides (allocated with
-the scales of one K block side by side, the order the products read).  Work and
+scales are float32 [rows, ceil(K/128)] tensors of any strides (as outputs, of any that
+keep the elements apart; allocated with the scales of one K block side by side, the
+order the products read).  An output may not overlap an input.  Work and
 allocations go to `stream`, the current one by default.
 """
 
@@ -80,7 +81,8 @@ def fp8_block_linear(a, a_scale, w, w_scale, out=None, out_dtype=torch.bfloat16,
     """out [M, N] = (a * a_scale) . (w * w_scale)^T.
 
     a codes [M, K], a_scale float32 [M, ceil(K/128)], w codes [N, K], w_scale
-    float32 [ceil(N/128), ceil(K/128)]; K and the row strides multiples of 16."""
+    float32 [ceil(N/128), ceil(K/128)]; K and the row strides multiples of 16.  out: a
+    bfloat16 or float16 tensor, whose own type then counts."""
     return _on(stream, a, _native.fp8_block_linear, a, a_scale, w, w_scale, out,
                _out_code(out_dtype))
 

@@ -87,6 +87,7 @@ int rms_norm_fp8(const fp8block_norm_args* args, void* stream);
  * [I, 2I).  h is not rounded in between; SiLU of a gate below -108.67, less than half
  * of the smallest float32, is -0.  codes [M, I] bytes, row stride ldc; scales [M, ceil(I/128)].
  * row_count (device, NULL = M): rows at or past it are not written.  M >= 0, I >= 1, M * ceil(I/128) < 2^31.
+ * codes and scales may not overlap gate_up or each other.
  */
 int swiglu_fp8(int dtype, const void* gate_up, int M, int I, int64_t ldg,
                const int32_t* row_count, uint8_t* codes, int64_t ldc, float* scales,
@@ -107,7 +108,7 @@ int swiglu_fp8(int dtype, const void* gate_up, int M, int I, int64_t ldg,
  * stride ld_ws; out [rows, N] of out_dtype (FP8BLOCK_BF16 or _F16), row
  * stride ldo (elements).
  * K % 16 == 0, lda and ldw multiples of 16, a and w 16-byte aligned; N and the
- * row counts are free.
+ * row counts are free.  out may not overlap an operand.
  *
  * fp8_block_linear: rows [0, M), M <= a_rows.  The grouped fields are ignored.
  *
