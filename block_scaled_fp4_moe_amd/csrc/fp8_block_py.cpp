@@ -159,7 +159,8 @@ void count(Py_ssize_t n, Py_ssize_t want) {
   if (n != want) refuse(want, " arguments are wanted, got ", n);
 }
 
-// x, weight, eps, residual, residual_out, y, codes, scales, stream
+// x, weight, eps, residual, residual_out, y, codes (False: neither codes nor scales),
+// scales, stream
 PyObject* norm(PyObject* const* a, Py_ssize_t n) {
   count(n, 9);
   const at::Tensor& x = tensor(a[0], "x");
@@ -193,21 +194,22 @@ PyObject* norm(PyObject* const* a, Py_ssize_t n) {
     same_matrix(y, "y", x);
     p.y_out = y.data_ptr(), p.ldy = ld(y);
   }
-  quantized_out(a[6], a[7], M, K, x, codes, scales);
-  p.codes = static_cast<uint8_t*>(codes.data_ptr()), p.ldc = ld(codes);
-  p.scales = static_cast<float*>(scales.data_ptr());
-  p.scale_row = scales.stride(0), p.scale_blk = scales.stride(1);
+  if (a[6] != Py_False) {
+    quantized_out(a[6], a[7], M, K, x, codes, scales);
+    p.codes = static_cast<uint8_t*>(codes.data_ptr()), p.ldc = ld(codes);
+    p.scales = static_cast<float*>(scales.data_ptr());
+    p.scale_row = scales.stride(0), p.scale_blk = scales.stride(1);
+  }
   check(rms_norm_fp8(&p, stream_of(a[8])));
   PyObject* out = PyTuple_New(3);
   if (!out) throw PythonError();
-  PyTuple_SET_ITEM(out, 0, give(a[6], codes));
-  PyTuple_SET_ITEM(out, 1, give(a[7], scales));
-  if (res_out.defined()) {
-    PyTuple_SET_ITEM(out, 2, give(a[4], res_out));
-  } else {
-    Py_INCREF(Py_None);
-    PyTuple_SET_ITEM(out, 2, Py_None);
-  }
+  auto put = [&](int at, PyObject* given, const at::Tensor& t) {
+    if (!t.defined()) Py_INCREF(Py_None);
+    PyTuple_SET_ITEM(out, at, t.defined() ? give(given, t) : Py_None);
+  };
+  put(0, a[6], codes);
+  put(1, a[7], scales);
+  put(2, a[4], res_out);
   return out;
 }
 

@@ -49,7 +49,7 @@ def _on(stream, lead, function, *args):
 
 
 def rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, codes=None,
-                 scales=None, stream=None):
+                 scales=None, stream=None, quantize=True):
     """v = x + residual; y = v * weight / sqrt(mean(v^2) + eps), quantized 1x128.
 
     x, residual [M, K] and weight [K] of one dtype (bfloat16, float16 or
@@ -57,7 +57,12 @@ def rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, 
     residual_out): residual_out is v rounded to the dtype (None without a
     residual; a new tensor unless one is passed).  y: a tensor that receives the
     normalised rows in the dtype.  residual_out and y may each be x or residual itself;
-    any other overlap of an output is refused."""
+    any other overlap of an output is refused.  quantize=False: y and residual_out alone
+    are written (for a layer that takes the rows themselves); codes and scales are None."""
+    if not quantize:
+        if codes is not None or scales is not None:
+            raise ValueError("codes and scales are not written with quantize=False")
+        codes = False
     return _on(stream, x, _native.rms_norm_fp8, x, weight, eps, residual, residual_out, y, codes,
                scales)
 

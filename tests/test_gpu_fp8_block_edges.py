@@ -140,3 +140,21 @@ def test_an_output_that_does_not_fit(gpu_lib):
     with pytest.raises(torch.OutOfMemoryError):
         gpu_lib.fp8_block_linear(a, sa, w, sw)               # 32 TiB
     assert not bool(gpu_lib.fp8_block_linear(a[:3].contiguous(), sa[:3], w, sw).any())
+
+
+@pytest.mark.parametrize("K", [640, 7168, 20480])
+def test_norm_for_a_layer_that_takes_the_rows(gpu_lib, K):
+    """quantize=False: y and the residual stream as with codes; nothing else is asked for."""
+    g = gen(K + 1)
+    x, r = randn(g, 9, K).bfloat16().cuda(), randn(g, 9, K).bfloat16().cuda()
+    w = (1 + 0.3 * randn(g, K)).bfloat16().cuda()
+    y, y2 = torch.empty_like(x), torch.empty_like(x)
+    _, _, ro = gpu_lib.rms_norm_fp8(x, w, residual=r, y=y)
+    c, s, ro2 = gpu_lib.rms_norm_fp8(x, w, residual=r, y=y2, quantize=False)
+    assert c is None and s is None and torch.equal(ro, ro2) and torch.equal(y, y2)
+    c, s, none = gpu_lib.rms_norm_fp8(x, w, y=x, quantize=False)
+    assert c is None and none is None
+    with pytest.raises(ValueError):
+        gpu_lib.rms_norm_fp8(x, w, y=y, scales=torch.empty((9, K // 128), device="cuda"), quantize=False)
+    with pytest.raises(gpu_lib.FP4MoEError):              # nothing to write
+        gpu_lib.rms_norm_fp8(x, w, quantize=False)
